@@ -19,8 +19,10 @@
 //          <b, b> = sum_p a_p B_p, P = sum_p a_p S_p): the term p = q drops
 //          out, so a token with one row, whose weight the norm makes almost
 //          irrelevant, gets its eps-sized gradient and not the difference of
-//          two large sums; formed as S_q sum a_p B_p - B_q sum a_p S_p in
-//          64 bits, where that term cancels to 2^-52 of itself
+//          two large sums.  Formed term by term in 64 bits, where products of
+//          two fp32 numbers are exact and the term p = q is 0, and rounded
+//          after the factor gate rho^3: the sum alone grows with the cube of z
+//          and leaves the range of fp32 for |z| from 10^12 on
 //   dw_post = sum_t gate D b rho,  dw_next = sum_t dh y sigma
 // The norms' statistics are formed again from b and y (the rows are read
 // anyway).  The token's rows of z are held in registers as loaded, so the two
@@ -550,13 +552,10 @@ __global__ __launch_bounds__(WAVE ? 256 : K > 4 ? kNormThreads / 2 : kNormThread
     }
     // The rows' weights: lane q has row q (a wave of the block).
     if (p.d_weight != nullptr && g0 < kWave) {
-      double by_s = 0.0, by_b = 0.0;  // sum_p a_p S_p, sum_p a_p B_p
       float sq = 0.f, bq = 0.f;
       int listed = 0, before = 0;
 #pragma unroll
       for (int o = 0; o < K; ++o) {
-        by_s = __builtin_fma(static_cast<double>(a[o]), static_cast<double>(s[2 + o]), by_s);
-        by_b = __builtin_fma(static_cast<double>(a[o]), static_cast<double>(s[2 + K + o]), by_b);
         sq = lane_id() == o ? s[2 + o] : sq;
         bq = lane_id() == o ? s[2 + K + o] : bq;
         const int same = rid[o] == mine ? 1 : 0;
@@ -564,8 +563,14 @@ __global__ __launch_bounds__(WAVE ? 256 : K > 4 ? kNormThreads / 2 : kNormThread
         before += lane_id() > o ? same : 0;
       }
       if (mine >= 0 && before == 0) {
-        const double da = static_cast<double>(p.eps) * sq + (sq * by_b - bq * by_s) * inv_h;
-        p.d_weight[mine] = static_cast<float>(listed) * gr * rho * rho * static_cast<float>(da);
+        double cross = 0.0;
+#pragma unroll
+        for (int o = 0; o < K; ++o) {
+          const double back = static_cast<double>(s[2 + o]) * bq;
+          cross = __builtin_fma(a[o], __builtin_fma(sq, static_cast<double>(s[2 + K + o]), -back), cross);
+        }
+        const double r = rho, da = static_cast<double>(p.eps) * sq + cross * inv_h;
+        p.d_weight[mine] = static_cast<float>(listed * static_cast<double>(gate) * r * r * r * da);
       }
     }
 #pragma unroll

@@ -9,6 +9,9 @@ second norm's statistic, then for D, b, the two sums and the products that
 follow, each at most 64: 256; a weight gradient adds at most T tokens in
 sequence per block and 16 + blocks / 16 partial sums."""
 
+import math
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -446,3 +449,45 @@ def test_a_bound_backward_needs_its_workspace():
     with pytest.raises(ValueError, match="workspace"):
         ops.combine_norm_backward(c["dy"], c["dh"], c["z"], c["rows"], c["row_weight"], c["x"], c["w_post"],
                                   c["w_next"], gate=c["gate"], bind=True)
+
+
+def _exact_row_gradients(s, eps):
+    """d_row_weight from dy in rational numbers, only the reciprocal norm's
+    root rounded: a token's only row has 1 / (1 + mean(b^2) / eps) of its
+    terms left, which 64-bit sums lose."""
+    num = lambda v: [Fraction(float(x)) for x in v]  # noqa: E731
+    dot = lambda a, b: sum(x * y for x, y in zip(a, b))  # noqa: E731
+    H = s["x"].shape[1]
+    out = torch.zeros(s["z"].shape[0], dtype=torch.float64)
+    for t in range(s["rows"].shape[0]):
+        ids = [r for r in s["rows"][t].tolist() if r >= 0]
+        if not ids:
+            continue
+        z = {r: num(s["z"][r]) for r in ids}
+        a = {r: Fraction(float(s["row_weight"][r])) for r in ids}
+        b = [sum(a[r] * z[r][i] for r in ids) for i in range(H)]
+        v = [x * y for x, y in zip(num(s["dy"][t]), num(s["w_post"]))]
+        rho2 = 1 / (dot(b, b) / H + Fraction(eps))
+        gate_rho = float(s["gate"][t]) * math.sqrt(rho2)
+        for r in ids:
+            out[r] = gate_rho * float(dot(v, z[r]) - dot(b, z[r]) * dot(v, b) * rho2 / H)
+    return out
+
+
+@pytest.mark.parametrize("size,eps", [(1e13, 1e-6), (1e16, 1e-6), (1e-15, 1e-30), (0.0, 1e-30)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_backward_of_large_and_small_rows(size, eps, dtype):
+    """Rows whose products with each other leave the range of fp32 when
+    multiplied once more, and a reciprocal norm whose cube does."""
+    say("combine_norm magnitudes", size, eps, dtype)
+    s = _inputs(24, 136, 3, dtype, seed=31)
+    s["z"] = (size * s["z"].double()).to(DT[dtype])
+    _, grad = _run(s, eps=eps, with_dh=False)
+    ref = close_grad_ref(d(s["dy"]), None, d(s["z"]), s["rows"], d(s["row_weight"]), None,
+                         d(s["w_post"]), None, d(s["gate"]), 0.75, eps)
+    listed = s["rows"][s["rows"] >= 0].long()
+    close_to(grad["d_row_weight"].cpu()[listed], _exact_row_gradients(s, eps)[listed],
+             ref["d_row_weight_size"][listed], 256, "d_row_weight")
+    for n in ("dx", "dz", "dw_post", "d_gate"):
+        at = listed if n == "dz" else slice(None)
+        close_to(grad[n].cpu()[at], ref[n][at], ref[n + "_size"][at], 256 + 24, n)
