@@ -765,8 +765,9 @@ def combine_norm_backward(dy: Optional[torch.Tensor], dh: Optional[torch.Tensor]
     """moe_combine_norm_backward: the gradients of combine_norm from dy
     and/or dh (dh needs the forward's y and w_next).  Returns {"dx", "dz",
     "d_row_weight", "d_gate", "dw_post", "dw_next"}, None where the forward
-    has no such input; rows of dz and d_row_weight that no token lists are
-    left as they are (allocated here: uninitialised)."""
+    has no such input (without dh, dw_next is zeros); rows of dz and
+    d_row_weight that no token lists are left as they are (allocated here:
+    uninitialised)."""
     ref = dy if dy is not None else dh
     if ref is None:
         raise ValueError("give dy, dh or both")
@@ -786,7 +787,7 @@ def combine_norm_backward(dy: Optional[torch.Tensor], dh: Optional[torch.Tensor]
         if row_weight is not None else None,
         "d_gate": _alloc_like(out, "d_gate", gate) if gate is not None else None,
         "dw_post": _alloc_like(out, "dw_post", w_post) if k else None,
-        "dw_next": _alloc_like(out, "dw_next", w_next) if dh is not None else None,
+        "dw_next": _alloc_like(out, "dw_next", w_next) if w_next is not None else None,
     }
     if ws is None:
         if bind:

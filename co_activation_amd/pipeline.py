@@ -792,8 +792,8 @@ class ExpertLayerBackward:
             ws=self._ffn_ws, d_err=s.d_err, bind=True)
 
     def run(self, dy, dh=None, timers: Optional[StageTimers] = None):
-        """``dy`` or ``dh`` may be None; ``dw_next`` is then as it was
-        without ``dh``."""
+        """``dy`` or ``dh`` may be None; without ``dh``, ``dw_next`` is
+        zeros."""
         step, s = self.step, self.step.side
         lp = step.layer.plan
         err, n = s.d_err, s.n_rows()

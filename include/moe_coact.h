@@ -567,7 +567,8 @@ int moe_expert_ffn_backward(const void* dy, const void* x, int64_t R, int64_t H,
  *              (t, j) is d_row_weight[slot_row[t*k+j]]
  *   d_gate     [T] float out or NULL (also meaningful when gate is NULL)
  *   dw_post, dw_next  [H] float out: summed over the tokens in an order that
- *              depends on the sizes alone; every element is written
+ *              depends on the sizes alone; every element is written (zeros
+ *              in dw_next without dh, in dw_post with k = 0)
  *   ws, ws_bytes  workspace of moe_combine_norm_backward_workspace_size()
  *              bytes, 16-byte aligned
  * The remaining arguments, limits and d_err bits are the forward's.  With

@@ -491,3 +491,20 @@ def test_backward_of_large_and_small_rows(size, eps, dtype):
     for n in ("dx", "dz", "dw_post", "d_gate"):
         at = listed if n == "dz" else slice(None)
         close_to(grad[n].cpu()[at], ref[n][at], ref[n + "_size"][at], 256 + 24, n)
+
+
+@pytest.mark.parametrize("H", [256, 4096])
+def test_the_next_norm_without_its_gradient(H):
+    """h was formed but nothing uses it: its weight's gradient is zero, and
+    what an earlier call left in the output is gone."""
+    c = _gpu(_inputs(40, H, 2, "bf16", seed=41))
+    y = ops.combine_norm(c["z"], c["rows"], c["row_weight"], c["x"], c["w_post"], c["w_next"])["y"]
+    out = {"dw_next": torch.full((H,), 7.0, device="cuda")}
+    args = (c["z"], c["rows"], c["row_weight"], y, c["w_post"], c["w_next"])
+    got = ops.combine_norm_backward(c["dy"], None, *args, out=out)
+    assert got["dw_next"] is out["dw_next"] and not bool(out["dw_next"].any())
+    out["dw_next"].fill_(7.0)
+    got = ops.combine_norm_backward(c["dy"], None, None, None, None, y, None, c["w_next"], out=out)
+    assert not bool(out["dw_next"].any()) and got["dw_post"] is None
+    plain = ops.combine_norm_backward(c["dy"], None, *args[:5])
+    assert plain["dw_next"] is None

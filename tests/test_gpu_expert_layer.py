@@ -296,3 +296,18 @@ def test_two_graphs_share_a_workspace_and_two_streams_do_not():
     for _, want, out, _ in cases:
         for k in want:
             assert torch.equal(out[k], want[k]), k
+
+
+def test_the_next_norm_gradient_of_an_earlier_run_does_not_stay():
+    w = make(1, T=130, H=64)
+    say("expert layer dw_next")
+    step, _ = _step(w, 48)
+    step.run()
+    dy, dh = _grads(step, 2)
+    back = ExpertLayerBackward(step)
+    back.run(dy, dh)
+    torch.cuda.synchronize()
+    assert bool(back.dw_next.any())
+    back.run(dy)
+    torch.cuda.synchronize()
+    assert not bool(back.dw_next.any())
