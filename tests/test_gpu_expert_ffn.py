@@ -448,3 +448,39 @@ def test_weight_tiles_dealt_out(E, H, F):
                                    c["count"], out=out)
     torch.cuda.synchronize()
     _check_backward(s, f["gu"].cpu(), f["a"].cpu(), {k: v.cpu() for k, v in grad.items()}, "silu")
+
+
+@pytest.mark.parametrize("rows", [1, 9, 200])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gelu_keeps_its_digits_in_the_tail(dtype, rows):
+    """The gates themselves as weights and a row of 1, 0, 0, ...: a is act(g)
+    and the first column of dw_in act'(g), each within a relative tolerance.
+    The exponential of -g^2 / 2 is off by the rounding of its argument, of the
+    argument in base 2 and of that base's constant, g^2 / 2 half steps each, and
+    its own; with the rest of the formula's roundings (64 counted) that is (2
+    g^2 + 64) half steps of Phi(g) and of |g| times the density."""
+    say("expert_ffn gelu tail", dtype, rows)
+    H, F = 8, 256
+    g = torch.cat((torch.linspace(-12, 4, F - 6), torch.tensor([0.0, -0.0, -1e-6, 1e-6, 40.0, 300.0])))
+    g = g.to(DT[dtype])
+    w_in = torch.zeros(1, 2 * F, H, dtype=DT[dtype])
+    w_in[0, :F, 0], w_in[0, F:, 0] = g, 1.0
+    w_down = torch.zeros(1, H, F, dtype=DT[dtype])
+    w_down[0, 0] = 1.0
+    x, dy = (torch.zeros(rows, H, dtype=DT[dtype]) for _ in range(2))
+    x[:, 0], dy[0, 0] = 1.0, 1.0
+    x, dy, w_in, w_down = (t.cuda() for t in (x, dy, w_in, w_down))
+    first, count = (torch.tensor([v], dtype=torch.int32, device="cuda") for v in (0, rows))
+    f = ops.expert_ffn(x, w_in, w_down, first, count, act="gelu", save=True)
+    b = ops.expert_ffn_backward(dy, x, w_in, w_down, f["gu"], f["a"], first, count, act="gelu")
+    torch.cuda.synchronize()
+    gd = g.double()
+    phi = 0.5 * torch.special.erfc(-gd / math.sqrt(2))
+    dens = torch.exp(-gd * gd / 2) / math.sqrt(2 * math.pi)
+    few = (2 * gd * gd + 64) * U32
+    for r in (0, rows - 1):
+        _bound(f["a"][r], gd * phi, few * gd.abs() * phi, "a")
+    value, slope = b["dw_in"][0, F:, 0], b["dw_in"][0, :F, 0]
+    again = HALF_STEP[DT[dtype]]  # [dg | du] lies in the workspace in the rows' type
+    _bound(value, gd * phi, (few + again) * gd.abs() * phi, "act")
+    _bound(slope, phi + gd * dens, few * (phi + gd.abs() * dens) + again * (phi + gd * dens).abs(), "slope")
