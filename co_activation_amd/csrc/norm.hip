@@ -817,7 +817,7 @@ extern "C" int moe_combine_norm(const void* z, int64_t z_rows, const int32_t* ro
   p.h_out = static_cast<moe::u32x4*>(h);
   p.rows = rows;
   p.weight = row_weight;
-  p.gate = gate;
+  p.gate = k > 0 ? gate : nullptr;
   p.w_post = k > 0 ? w_post : nullptr;
   p.w_next = h != nullptr ? w_next : nullptr;
   p.n_valid = n_valid;

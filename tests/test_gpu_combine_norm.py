@@ -508,3 +508,21 @@ def test_the_next_norm_without_its_gradient(H):
     assert not bool(out["dw_next"].any()) and got["dw_post"] is None
     plain = ops.combine_norm_backward(c["dy"], None, *args[:5])
     assert plain["dw_next"] is None
+
+
+@pytest.mark.parametrize("H", [256, 4096])
+def test_without_a_block_its_arguments_are_not_read(H):
+    """k = 0: a gate shorter than the tokens and full of NaN, as the C
+    interface may be given it, plays no part."""
+    say("combine_norm k = 0", H)
+    c = _gpu(_inputs(700, H, 1, "bf16", seed=43))
+    want = ops.combine_norm(None, None, None, c["x"], None, c["w_next"], residual_scale=0.75)
+    got = {n: torch.empty_like(c["x"]) for n in ("y", "h")}
+    gate = torch.full((1,), float("nan"), device="cuda")
+    st = ops._lib.lib().moe_combine_norm(
+        None, 0, None, 0, None, c["x"].data_ptr(), gate.data_ptr(), None, c["w_next"].data_ptr(), 0.75,
+        1e-6, 700, H, 1, got["y"].data_ptr(), got["h"].data_ptr(), None, None,
+        torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    for n in got:
+        assert torch.equal(got[n], want[n]), n
