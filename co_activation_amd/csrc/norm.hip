@@ -476,6 +476,7 @@ __global__ __launch_bounds__(WAVE ? 256 : K > 4 ? kNormThreads / 2 : kNormThread
     }
     load_rows(t + step);
     if (p.k == 0) {
+      if (g0 == 0 && p.d_gate != nullptr) p.d_gate[t] = 0.f;
       if (!WAVE && p.dh != nullptr) __syncthreads();  // s_sum[0]
       continue;
     }

@@ -526,3 +526,25 @@ def test_without_a_block_its_arguments_are_not_read(H):
     assert st == 0
     for n in got:
         assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("H", [256, 4096])
+@pytest.mark.parametrize("with_dh", [True, False])
+def test_the_gate_gradient_without_a_block_is_zero(H, with_dh):
+    """The C interface may ask for it: every token's is written, those from
+    n_valid on stay."""
+    say("combine_norm k = 0 d_gate", H, with_dh)
+    T, n = 2500, 2311
+    c = _gpu(_inputs(T, H, 1, "bf16", seed=44))
+    d_gate = torch.full((T,), 7.0, device="cuda")
+    n_valid = torch.tensor([n], dtype=torch.int32, device="cuda")
+    dx, dw = torch.empty_like(c["x"]), torch.empty(H, device="cuda")
+    ws = torch.empty(ops.combine_norm_workspace_bytes(T, H, torch.bfloat16), dtype=torch.uint8, device="cuda")
+    p = lambda t: t.data_ptr()  # noqa: E731
+    st = ops._lib.lib().moe_combine_norm_backward(
+        p(c["dy"]), p(c["dh"]) if with_dh else None, None, 0, None, 0, None, p(c["x"]), None, None,
+        p(c["w_next"]), 0.75, 1e-6, T, H, 1, p(dx), None, None, p(d_gate), None, p(dw), p(n_valid),
+        None, p(ws), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0
+    assert not bool(d_gate[:n].any()) and bool((d_gate[n:] == 7.0).all())
