@@ -1422,8 +1422,9 @@ int ffn_check(int64_t R, int64_t H, int64_t F, int E, int dtype, int act) {
   if (act != MOE_ACT_SILU && act != MOE_ACT_GELU) return MOE_ERR_DTYPE;
   const int64_t es = dtype == MOE_BF16 ? 2 : 4;
   // One expert's projections, and a tile's rows, are addressed through
-  // 32-bit byte offsets.
-  if (R < 0 || R > INT32_MAX || E < 1 || E > MOE_MAX_E || H <= 0 || F <= 0 || H > (1 << 21) ||
+  // 32-bit byte offsets; rows are counted in 32 bits and rounded up to whole
+  // tiles and ranges (of 256 at most).
+  if (R < 0 || R > INT32_MAX - 511 || E < 1 || E > MOE_MAX_E || H <= 0 || F <= 0 || H > (1 << 21) ||
       F > (1 << 20) || 2 * F * H * es >= kOut)
     return MOE_ERR_SHAPE;
   if (H * es % 16 != 0 || F * es % 16 != 0) return MOE_ERR_ALIGN;

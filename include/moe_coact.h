@@ -500,8 +500,8 @@ int moe_place_experts(const float* coact /* host */, const float* load /* host *
  * g and u.
  * Limits: 1 <= E <= 256, H and F row multiples of 16 bytes, buffers 16-byte
  * aligned, H <= 2^21, F <= 2^20, one expert's w_in smaller than 2^31 - 256
- * bytes, R < 2^31; an output that overlaps an input or another output is refused
- * (MOE_ERR_SHAPE).  Blocks of rows that overlap give unspecified rows.
+ * bytes, R <= 2^31 - 512; an output that overlaps an input or another output
+ * is refused (MOE_ERR_SHAPE).  Blocks of rows that overlap give unspecified rows.
  * d_err bits: EXPERT_ROWS.
  *
  * moe_expert_ffn_backward -- its gradients:

@@ -121,3 +121,15 @@ def test_expert_ffn_workspace(built_lib):
     assert q(100, 64, 32, 2, 1, NULL) == -1 and q(-1, 64, 32, 2, 1, ctypes.byref(n)) == -2
     assert q(100, 64, 36, 2, 1, ctypes.byref(n)) == -4 and q(100, 64, 32, 2, 9, ctypes.byref(n)) == -3
     assert q(100, 64, 32, 0, 1, ctypes.byref(n)) == -2
+
+
+def test_expert_ffn_most_rows(built_lib):
+    """Row counts are rounded up to whole tiles in 32 bits: the last 511
+    counts are refused (a missing pointer tells an accepted size)."""
+    n = ctypes.c_size_t()
+    size = built_lib.moe_expert_ffn_backward_workspace_size
+    most = 2 ** 31 - 512
+    assert _ffn(built_lib, R=most, x=NULL) == -1 and _ffn(built_lib, R=most + 1, x=NULL) == -2
+    assert _ffn_grad(built_lib, R=most, x=NULL) == -1 and _ffn_grad(built_lib, R=most + 1, x=NULL) == -2
+    assert size(most, 8, 8, 1, 1, ctypes.byref(n)) == 0 and n.value >= most * 32
+    assert size(2 ** 31 - 1, 8, 8, 1, 1, ctypes.byref(n)) == -2
