@@ -1484,7 +1484,8 @@ extern "C" int moe_expert_ffn(const void* x, int64_t R, int64_t H, int64_t F, in
   const int64_t es = dtype == MOE_BF16 ? 2 : 4;
   const int64_t w = E * H * F * es;
   if (moe::any_overlap({{gu, R * 2 * F * es}, {a, R * F * es}, {y, R * H * es}},
-                       {{x, R * H * es}, {w_in, 2 * w}, {w_down, w}}))
+                       {{x, R * H * es}, {w_in, 2 * w}, {w_down, w}, {expert_first, E * int64_t{4}},
+                        {expert_count, E * int64_t{4}}}))
     return MOE_ERR_SHAPE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const moe::ExpertRows rows = {expert_first, expert_count, d_err, E, static_cast<int>(R)};
@@ -1526,7 +1527,7 @@ extern "C" int moe_expert_ffn_backward(const void* dy, const void* x, int64_t R,
   if (ws_bytes < static_cast<size_t>(space.all)) return MOE_ERR_WORKSPACE;
   if (moe::any_overlap({{dx, R * H * es}, {dw_in, 2 * w}, {dw_down, w}, {ws, space.all}},
                        {{dy, R * H * es}, {x, R * H * es}, {w_in, 2 * w}, {w_down, w}, {gu, dgu},
-                        {a, dgu / 2}}))
+                        {a, dgu / 2}, {expert_first, E * int64_t{4}}, {expert_count, E * int64_t{4}}}))
     return MOE_ERR_SHAPE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const moe::ExpertRows rows = {expert_first, expert_count, d_err, E, static_cast<int>(R)};

@@ -133,3 +133,13 @@ def test_expert_ffn_most_rows(built_lib):
     assert _ffn_grad(built_lib, R=most, x=NULL) == -1 and _ffn_grad(built_lib, R=most + 1, x=NULL) == -2
     assert size(most, 8, 8, 1, 1, ctypes.byref(n)) == 0 and n.value >= most * 32
     assert size(2 ** 31 - 1, 8, 8, 1, 1, ctypes.byref(n)) == -2
+
+
+def test_expert_ffn_outputs_over_the_counts(built_lib):
+    """expert_first and expert_count are inputs too."""
+    at = 6 * FAR
+    for n in ("first", "count"):
+        for out in ("gu", "a", "y"):
+            assert _ffn(built_lib, **{n: at + 4, out: at}) == -2, (n, out)
+        for out in ("dx", "dwi", "dwd", "ws"):
+            assert _ffn_grad(built_lib, **{n: at + 4, out: at}) == -2, (n, out)
