@@ -869,14 +869,18 @@ extern "C" int moe_combine_norm_backward(
   moe_combine_norm_backward_workspace_size(T, H, dtype, &need);
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   const int64_t row = H * (dtype == MOE_BF16 ? 2 : 4);
-  const void* in[4] = {dy, dh, dh != nullptr ? y : nullptr, nullptr};
+  const int64_t space = static_cast<int64_t>(need);
+  const void* in[3] = {dy, dh, dh != nullptr ? y : nullptr};
   for (const void* i : in)
-    if (moe::overlap(dx, T * row, i, T * row) ||
+    if (moe::overlap(dx, T * row, i, T * row) || moe::overlap(ws, space, i, T * row) ||
         (k > 0 && moe::overlap(dz, z_rows * row, i, T * row)))
       return MOE_ERR_SHAPE;
+  if (moe::overlap(ws, space, dx, T * row)) return MOE_ERR_SHAPE;
   if (k > 0 && (moe::overlap(dx, T * row, z, z_rows * row) ||
                 moe::overlap(dx, T * row, dz, z_rows * row) ||
-                moe::overlap(dz, z_rows * row, z, z_rows * row)))
+                moe::overlap(dz, z_rows * row, z, z_rows * row) ||
+                moe::overlap(ws, space, z, z_rows * row) ||
+                moe::overlap(ws, space, dz, z_rows * row)))
     return MOE_ERR_SHAPE;
   hipStream_t st = static_cast<hipStream_t>(stream);
   moe::NormArgs p = {};

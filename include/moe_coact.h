@@ -571,7 +571,7 @@ int moe_expert_ffn_backward(const void* dy, const void* x, int64_t R, int64_t H,
  *              depends on the sizes alone; every element is written (zeros
  *              in dw_next without dh, in dw_post with k = 0)
  *   ws, ws_bytes  workspace of moe_combine_norm_backward_workspace_size()
- *              bytes, 16-byte aligned
+ *              bytes, 16-byte aligned, apart from every row buffer
  * The remaining arguments, limits and d_err bits are the forward's.  With
  * n_valid, tokens from *n_valid on are not read and add nothing.
  * ---------------------------------------------------------------------- */

@@ -143,3 +143,10 @@ def test_expert_ffn_outputs_over_the_counts(built_lib):
             assert _ffn(built_lib, **{n: at + 4, out: at}) == -2, (n, out)
         for out in ("dx", "dwi", "dwd", "ws"):
             assert _ffn_grad(built_lib, **{n: at + 4, out: at}) == -2, (n, out)
+
+
+def test_combine_norm_workspace_over_rows(built_lib):
+    """The workspace shares no bytes with a row buffer."""
+    at = 6 * FAR
+    for n in ("dy", "dh", "y", "z", "dx", "dz"):
+        assert _grad(built_lib, ws=at, **{n: at + 64}) == -2, n
