@@ -876,6 +876,8 @@ extern "C" int moe_combine_norm_backward(
         (k > 0 && moe::overlap(dz, z_rows * row, i, T * row)))
       return MOE_ERR_SHAPE;
   if (moe::overlap(ws, space, dx, T * row)) return MOE_ERR_SHAPE;
+  // A token's gate is read by all waves of its block, one of which writes d_gate.
+  if (moe::overlap(d_gate, T * 4, gate, T * 4)) return MOE_ERR_SHAPE;
   if (k > 0 && (moe::overlap(dx, T * row, z, z_rows * row) ||
                 moe::overlap(dx, T * row, dz, z_rows * row) ||
                 moe::overlap(dz, z_rows * row, z, z_rows * row) ||

@@ -566,7 +566,7 @@ int moe_expert_ffn_backward(const void* dy, const void* x, int64_t R, int64_t H,
  *              where no token lists the row; the gate gradient of slot
  *              (t, j) is d_row_weight[slot_row[t*k+j]]
  *   d_gate     [T] float out or NULL (also meaningful when gate is NULL;
- *              zeros with k = 0)
+ *              zeros with k = 0); not over gate (MOE_ERR_SHAPE)
  *   dw_post, dw_next  [H] float out: summed over the tokens in an order that
  *              depends on the sizes alone; every element is written (zeros
  *              in dw_next without dh, in dw_post with k = 0)

@@ -150,3 +150,9 @@ def test_combine_norm_workspace_over_rows(built_lib):
     at = 6 * FAR
     for n in ("dy", "dh", "y", "z", "dx", "dz"):
         assert _grad(built_lib, ws=at, **{n: at + 64}) == -2, n
+
+
+def test_combine_norm_gate_gradient_over_the_gate(built_lib):
+    """Waves of a token's block read its gate after another has written."""
+    at = 6 * FAR
+    assert _grad(built_lib, gate=at, dg=at) == -2 and _grad(built_lib, gate=at + 12, dg=at) == -2
