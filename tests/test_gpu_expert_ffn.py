@@ -143,6 +143,7 @@ def _run(s, owned, act, save=True, backward=True):
     ([5, 0, 16, 15, 2, 1, 33, 0], 264, 136, "silu"),
     ([70, 1, 64, 129], 200, 328, "gelu"),       # K and N tails of every tile
     ([100, 300, 0, 150], 520, 264, "silu"),
+    # (as few tiles as here are 128 x 64; test_gpu_expert_tiles.py has the wide ones)
     ([700, 513], 136, 392, "silu"),             # the widest row tiles
     ([257], 1024, 512, "gelu"),
     ([3100], 40, 24, "silu"),                   # the rows of a weight gradient in ranges
@@ -169,6 +170,7 @@ def test_many_experts_in_another_order(dtype):
 def test_every_row_tile(counts):
     """The tile a launch takes goes by the rows an expert has on average:
     uneven experts fill it badly and stay right."""
+    # (all of these are few enough to be 128 x 64; test_gpu_expert_tiles.py has the others)
     for pad in (0, 1500):  # more rows of no expert: another tile
         s, owned = _inputs(counts, 96, 160, "bf16", seed=pad, gap=pad // len(counts))
         say("expert_ffn tiles", counts, pad)
