@@ -311,3 +311,59 @@ def test_the_next_norm_gradient_of_an_earlier_run_does_not_stay():
     back.run(dy)
     torch.cuda.synchronize()
     assert not bool(back.dw_next.any())
+
+
+def _balanced(w, seed, weights, fused):
+    """cfg 5's routing with fp32 rows through a balanced two-layer step."""
+    g = torch.Generator().manual_seed(seed)
+    T, H, F, E = w.T, w.H, 48, w.E
+    rnd = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    layer = TwoLayerStep(i32(w.topk), i32(w.topk2), dev(w.gates2), i32(w.expert_rank2), rnd(T, H),
+                         torch.zeros(1, H, device="cuda"), w.G, w.ranks_per_node, E1=w.E,
+                         balanced=True, fused=fused)
+    if weights is None:
+        weights = [rnd(E, 2 * F, H) / math.sqrt(H), rnd(E, H, F) / math.sqrt(F), 1 + 0.1 * rnd(H),
+                   1 + 0.1 * rnd(H), torch.rand(T, generator=g).cuda()]
+    w_in, w_down, w_post, w_next, gate = weights
+    return ExpertLayerStep(layer, w_in, w_down, w_post, w_next, gate=gate, residual_scale=0.75), weights
+
+
+@pytest.mark.parametrize("beside", ["combine", "move"])
+@pytest.mark.parametrize("fused", [True, False])
+def test_balanced_two_layer_batches_through_a_pipeline(beside, fused):
+    """Each batch against the layer in 64 bits over its own shuffled rows,
+    forward and backward, then the same batches through a pipeline."""
+    ws = [make(5, T=192, H=64, seed=s) for s in (3, 4)]
+    say("expert layer balanced pipeline", beside, fused)
+    first, weights = _balanced(ws[0], 1, None, fused)
+    steps = [first, _balanced(ws[1], 2, weights, fused)[0]]
+    H, F, T, k = 64, 48, 192, ws[0].k
+    terms = [H, F, k, H, H]
+    tol_y = U32 * (sum(K ** 1.5 for K in terms) + 64)
+    terms += [H, H, k, H, 2 * F, T]
+    tol = U32 * (sum(K ** 1.5 for K in terms) + 192)
+    want = []
+    for st in steps:
+        st.run()
+        back = ExpertLayerBackward(st)
+        dy, dh = _grads(st, 5)
+        back.run(dy, dh)
+        torch.cuda.synchronize()
+        assert int(st.d_err.item()) == 0
+        layer = st.layer
+        assert torch.equal(torch.sort(layer.shuffle["perm"]).values, torch.arange(T, device="cuda").int())
+        assert torch.equal(layer.x_s, layer.x[layer.shuffle["perm"].long()])
+        y, h, grads = _whole(None, st, dy, dh, layer.topk2_s.cpu().long(), layer.gates2_s, layer.x_s)
+        got = {"x": back.dx, "res": back.d_residual, "gates": back.dw, "w_in": back.dw_in,
+               "w_down": back.dw_down, "w_post": back.dw_post, "w_next": back.dw_next, "gate": back.d_gate}
+        for name, a, b, t in [("y", st.y, y, tol_y), ("h", st.h, h, tol_y)] + \
+                [("d_" + n, got[n], grads[n], tol) for n in got]:
+            off = float((d(a) - b).norm() / b.norm())
+            assert off <= t, f"{name}: off by {off:.3g} of its norm, allowed {t:.3g}"
+        want.append((st.y.clone(), st.h.clone()))
+    seen = []
+    Pipeline(steps, beside).run(6, collect=lambda st, i: seen.append((i, st.y.clone(), st.h.clone())))
+    torch.cuda.synchronize()
+    assert all(int(st.d_err.item()) == 0 for st in steps) and len(seen) == 6
+    for i, y, h in seen:
+        assert torch.equal(y, want[i % 2][0]) and torch.equal(h, want[i % 2][1])
