@@ -20,10 +20,10 @@
 // host never waits for the routing: every block cuts the experts' rows into
 // tiles from the counts and finds its own.
 //
-// Measured on MI355X (bf16): 65536 rows over 64 experts of 4096 x 2048, 3.2 ms
-// forward (1.03 PFLOP/s), 6.55 backward (1.0); 24594 uneven rows over 128 of
-// 2048 x 1000, 0.54 and 1.35 ms; one token's eight experts of 4096 x 2048,
-// 71 us (weights at 5.7 TB/s).
+// Measured on MI355X (bf16): 65536 rows over 64 experts of 4096 x 2048, 3.25 ms
+// forward (1.01 PFLOP/s), 6.65 backward (0.99); 24594 uneven rows over 128 of
+// 2048 x 1000, 0.53 and 1.3 to 1.4 ms; one token's eight experts of 4096 x 2048,
+// 74 us (weights at 5.4 TB/s).
 #include <initializer_list>
 
 #include "gemm.hpp"
@@ -1248,7 +1248,7 @@ inline int f32_tile(int64_t rows, int64_t cols) {
 // Which tile, measured on MI355X (bf16, time of forward / backward):
 //  - up to one row an expert on average: the few-rows kernel (rows routed at
 //    random, forward: 64 experts of 4096 x 2048, 48 rows in all 288 us, tiles
-//    of 128 346; 8 of 4096 x 8192, 8 rows 176 and 247; with two rows an
+//    of 128 346 side by side (280 to 320 by routing and card); 8 of 4096 x 8192, 8 rows 176 and 247; with two rows an
 //    expert 546 and 476, 286 and 282);
 //  - from 512 rows an expert, with a tile for half the CUs: 256 x 256, fewest
 //    bytes a product (64 experts of 4096 x 2048, 1024 rows: 3.19 / 6.34 ms

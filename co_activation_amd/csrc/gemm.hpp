@@ -1,10 +1,14 @@
 // Grouped matrix products on MFMA tiles (bf16 in, fp32 accumulation), the
 // machinery of the experts' feed-forward block (ffn.hip).  Measured on MI355X,
 // 64 experts of 4096 x 2048 with 1024 rows each on average: up 2.2 ms (1.0
-// PFLOP/s), down 1.15 (0.95), activation gradient 1.2 (0.91), dx 1.95 (1.13),
-// dWin 2.35 (0.94), dWdown 1.13 (0.97); MFMAs are issued in 50 to 65% of a CU's
-// cycles.  What bounds a step is the way from L2 into LDS: 64 KiB a step of 64
-// k take 1.5 us, the matrix work on them 1.0.
+// PFLOP/s), down 1.13 (0.97), activation gradient 1.23 (0.89), dx 2.0 (1.1),
+// dWin 2.34 (0.94), dWdown 1.13 (0.97).  MFMAs are issued in 51 to 66% of a CU's
+// cycles: a step of 64 k of up takes 1.5 us, its matrix work 1.0.  The rest is
+// waiting and not the rate of the way from L2 into LDS: up and down, with two
+// stages of 64 k whose loads all go out in the first of a step's two memory
+// turns, have their waves wait (loads and barriers) 36% of the time and take 0.13
+// cache lines a CU and cycle from L2; dx, with four stages of 32 k, waits 25% and
+// takes 0.22.
 //
 // A block of WM x WN waves computes a BM x BN tile of C = A B, held as 16x16
 // accumulators: MF row fragments (every WM-th one of the tile, so that a tile

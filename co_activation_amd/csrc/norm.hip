@@ -26,9 +26,10 @@
 //   dw_post = sum_t gate D b rho,  dw_next = sum_t dh y sigma
 // The norms' statistics are formed again from b and y (the rows are read
 // anyway).  The token's rows of z are held in registers as loaded, so the two
-// passes over them (b, then the dot products) cost one read; a block walks
-// tokens and keeps the weight gradients in registers, and its sums go to the
-// workspace once, where a second kernel adds them in a fixed order.
+// passes over them (b, then the dot products) cost one read (two where k > 4
+// and rows are over 16 KiB); a block walks tokens and keeps the weight
+// gradients in registers or LDS, and its sums go to the workspace once, where
+// a second kernel adds them in a fixed order.
 //
 // Both kernels are a chain a token: row ids, rows, a sum over the row, and
 // stores.  So they load one token ahead: the next token's row ids come with
@@ -43,12 +44,21 @@
 // once, when stored.
 //
 // Measured on MI355X, bf16, all inputs and outputs given.  Forward: 65536
-// tokens, rows of 4096, two a token: 454 us for 2.62 GB, 5.8 TB/s (a copy
+// tokens, rows of 4096, two a token: 455 us for 2.62 GB, 5.8 TB/s (a copy
 // reaches 6.6); 32768 tokens, rows of 7168, eight a token: 915 us, 5.6 TB/s.
 // Backward: the same 65536 tokens 843 us for 4.3 GB, 5.1 TB/s; 16384 tokens,
-// rows of 7168, eight a token 919 us, 5.0 TB/s.  Vector instructions fill a
-// good half of the backward's time, which is why its sums go four at a time
-// and its weights through buffers.
+// rows of 7168, eight a token 920 us, 5.0 TB/s.  fp32, 32768 tokens, rows of
+// 4096, two a token: 455 us forward, 5.9 TB/s, 797 backward, 5.4 TB/s.  Vector
+// instructions fill a good half of the backward's time, which is why its sums
+// go four at a time and its weights through buffers.
+//
+// Rows that need two groups a thread or more do not fit the registers: the
+// compiler spills 16 (bf16, k <= 2), 54 (bf16, k <= 4) or 22 (fp32, k <= 4) of
+// the 128 that 1024 threads have (rows over 16 KiB), and 19 of the 256 that 512
+// have (bf16, k > 4, rows over 8 KiB; 8 over 16 KiB); of the forward 26 (bf16,
+// k > 4, rows over 16 KiB).  16384 tokens, bf16 rows of 16384, backward: two a
+// token 867 us, 5.0 TB/s, but four a token 2078 us, 3.1 TB/s; 8192 tokens, eight
+// a token 656 us forward, 4.5 TB/s, 1100 backward, 4.9 TB/s.
 #include <math.h>
 
 #include "rowio.hpp"

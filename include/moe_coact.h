@@ -502,6 +502,9 @@ int moe_place_experts(const float* coact /* host */, const float* load /* host *
  * aligned, H <= 2^21, F <= 2^20, one expert's w_in smaller than 2^31 - 256
  * bytes, R <= 2^31 - 512; an output that overlaps an input or another output
  * is refused (MOE_ERR_SHAPE).  Blocks of rows that overlap give unspecified rows.
+ * Kernels and tiles are chosen from R / E, since the counts stay on the device:
+ * R a little over the rows in use is right and fast, a buffer sized for the
+ * worst case is right but takes the tiles of a full one.
  * d_err bits: EXPERT_ROWS.
  *
  * moe_expert_ffn_backward -- its gradients:
