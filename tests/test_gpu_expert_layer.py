@@ -367,3 +367,50 @@ def test_balanced_two_layer_batches_through_a_pipeline(beside, fused):
     assert all(int(st.d_err.item()) == 0 for st in steps) and len(seen) == 6
     for i, y, h in seen:
         assert torch.equal(y, want[i % 2][0]) and torch.equal(h, want[i % 2][1])
+
+
+def test_a_captured_pipeline_follows_its_inputs():
+    from co_activation_amd.pipeline import GraphPipeline
+    say("expert layer graph pipeline")
+    ws = [make(5, T=192, H=128, seed=s) for s in (6, 7)]
+    first, weights = _step(ws[0], 64, train=False)
+    steps = [first, _step(ws[1], 64, train=False, weights=weights)[0]]
+    graph = GraphPipeline(Pipeline(steps), 4)
+    for seed in range(3):
+        g = torch.Generator().manual_seed(seed)
+        for st in steps:
+            st.layer.x.copy_(torch.randn(st.layer.x.shape, generator=g))
+        want = []
+        for st in steps:
+            st.run()
+            want.append((st.y.clone(), st.h.clone()))
+            st.y.zero_()
+            st.h.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for st, (y, h) in zip(steps, want):
+            assert int(st.d_err.item()) == 0
+            assert torch.equal(st.y, y) and torch.equal(st.h, h)
+
+
+@pytest.mark.parametrize("cfg", [1, 5])
+def test_stage_timers_cover_every_stage(cfg):
+    """The names that STAGES lists are those that a run records, each once,
+    alone and in a pipeline."""
+    from co_activation_amd.pipeline import StageTimers
+    say("expert layer timers", cfg)
+    first, weights = _step(make(cfg, T=192, H=64, seed=1), 48)
+    timers = StageTimers(first.STAGES, 1)
+    first.run(timers)
+    back = ExpertLayerBackward(first)
+    back_timers = StageTimers(back.STAGES, 1)
+    back.run(*_grads(first, 1), timers=back_timers)
+    torch.cuda.synchronize()
+    assert timers.used == {n: 1 for n in first.STAGES} and len(timers.mean_ms()) == len(first.STAGES)
+    assert back_timers.used == {n: 1 for n in back.STAGES}
+    second, _ = _step(make(cfg, T=192, H=64, seed=2), 48, weights=weights)
+    timers = StageTimers(first.STAGES, 6)
+    Pipeline([first, second], "combine").run(6, timers)
+    torch.cuda.synchronize()
+    assert timers.used == {n: 6 for n in first.STAGES}
